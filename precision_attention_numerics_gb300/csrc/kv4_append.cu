@@ -41,14 +41,16 @@ __device__ __forceinline__ uint2 quantise16(const float (&x)[16], float g, uint3
   s8 = cvt_e4m3x2(__fdiv_rn(am, __fmul_rn(6.0f, g)), 0.0f);
   const float den = __fmul_rn(g, e4m3x2_to_f2(uint16_t(s8)).x);
   uint32_t c[8];
-  if ((__float_as_uint(g) & 0x007FFFFFu) == 0u) {
+  if ((__float_as_uint(g) & 0x007FFFFFu) == 0u && am <= __fmul_rn(den, 1048576.0f)) {
     // g is a power of two (1 mostly), so den has four significant bits, and the
     // code of fl32(x / den) comes without a division: let T be x / den rounded to three
     // bits after the leading one.  All points where E2M1 changes are such T, so only
     // the side of T matters; e = x - T den (one rounding, exact in sign) tells it, and
     // if e is not 0, x / den is further from T than half its last place: x - T den is at
     // least one last place of x, whose leading digits are at most 1.875.  So z = T + e / den is T
-    // exactly when fl32(x / den) is, and on the same side otherwise.
+    // exactly when fl32(x / den) is, and on the same side otherwise.  Every step is finite up to
+    // |x| = 2^20 den; a block with larger values is divided, where x / den may overflow to an
+    // infinity of x's sign, which saturates.
     const float r = __fdiv_rn(1.0f, den);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
