@@ -379,8 +379,11 @@ attnq_status attnq_attention_host(const attnq_desc* desc, int32_t n_steps, const
  * exist.  Lengths and tables are read by the kernels, so a captured call follows
  * their current contents.  A page number outside the pool, or a length outside
  * its range, is recorded as ATTNQ_EPAGE: such tokens are neither read nor
- * written and count as masked, such a length is clamped.  Two sequences may share
- * pages as long as neither appends to them.
+ * written and count as masked, and attention and eviction clamp such a length.  attnq_kv4_append
+ * and attnq_kv4_read keep the places that a length past the table gives their
+ * rows, and drop the rows that it has no room for.  Two sequences may share
+ * pages as long as neither appends to them; a page that takes new rows stands once
+ * in the table.
  *
  * attnq_rows: rows of d contiguous elements of type dtype (ATTNQ_F32 or
  * ATTNQ_BF16); row t of head h of sequence b starts at element b * stride_b +

@@ -93,6 +93,11 @@ __device__ __forceinline__ int kv4_new(const Kv4Map& m, int b) {
   return n;
 }
 
+// Place of row 0 of the n new rows of sequence b, of length L as kv4_len gives it.  A length past the
+// page table (reported there) moves no row: rows whose place it has no room for are dropped,
+// and those before them do not land on other tokens.
+__device__ __forceinline__ int kv4_first(const Kv4Map& m, int b, int L, int n) { return max(m.lens[b], L) - n; }
+
 // Address of tile `tile` of sequence b, KV head h; null (and a status bit) for
 // a page number outside the pool.
 template <int D>

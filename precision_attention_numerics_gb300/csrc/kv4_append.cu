@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const AppendParam
   __shared__ __align__(16) uint32_t s_tile[kv4_tile_bytes(D) / 4];
   const int h = blockIdx.y % p.map.Hkv, b = blockIdx.y / p.map.Hkv;
   const int L = kv4_len(p.map, b), n = kv4_new(p.map, b);
-  const int first = L - n;  // place of row 0
+  const int first = kv4_first(p.map, b, L, n);  // place of row 0
+  if (first >= L) return;
   const int tile = max(first, 0) / kKv4Tile + int(blockIdx.x);
   // places of this tile that the call writes: [lo, hi)
   const int lo = max(max(first, 0) - tile * kKv4Tile, 0), hi = min(L - tile * kKv4Tile, kKv4Tile);
@@ -232,7 +233,8 @@ __global__ void __launch_bounds__(128) k_kv4_read(const ReadParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const bool is_v = warp & 1;
   const int L = kv4_len(p.map, b), n = kv4_new(p.map, b);
-  const int first = L - n;
+  const int first = kv4_first(p.map, b, L, n);  // place of row 0
+  if (first >= L) return;
   const int tile = max(first, 0) / kKv4Tile + int(blockIdx.x) * 2 + (warp >> 1);
   const int lo = max(max(first, 0) - tile * kKv4Tile, 0), hi = min(L - tile * kKv4Tile, kKv4Tile);
   if (lo >= hi) return;

@@ -35,3 +35,38 @@ def test_append_far_past_the_largest_value(g, dtype, rotate):
         most = 6 * 448 * g
         if amplitude > 1e6 * most and not rotate:
             assert (V[0, 0, :, :32].abs() == most).any() and (V[0, 0] == -most).any()
+
+
+@pytest.mark.parametrize("d,over,T", [(64, 1, 1), (64, 3, 8), (128, 20, 40), (64, 60, 40), (128, 2 ** 31 - 1 - 96, 5)])
+def test_append_past_the_page_table(d, over, T):
+    """A length past the table's capacity is reported; rows keep their places, those past the last place
+    are dropped, and no other token loses its bits."""
+    aq = _aq()
+    cap = 96
+    st = Setup([cap, 50], 2, d, 16, seed=over % 97)
+    st.table = st.table[:, :6].contiguous()  # exactly 96 places
+    gen = torch.Generator().manual_seed(T)
+    K, V = (torch.randn((2, 2, T, d), generator=gen).to(BF16) for _ in range(2))
+    lens = torch.tensor([cap + over, 50], dtype=torch.int32).cuda()
+    aq.attnq_kv4_append(st.cache, aq.AttnqKv4Seqs(st.table, lens), K.cuda(), V.cuda())
+    assert aq.attnq_device_status() == 6
+    whole = torch.tensor([cap, 50], dtype=torch.int32).cuda()
+    got = [torch.empty((2, 2, cap, d), device="cuda") for _ in range(2)]
+    aq.attnq_kv4_read(st.cache, aq.AttnqKv4Seqs(st.table, whole, whole), *got)
+    assert aq.attnq_device_status() == 0
+    for new, old, out in ((K, st.K, got[0]), (V, st.V, got[1])):
+        for b, L in ((0, cap + over), (1, 50)):
+            want = old[b, :, :min(L, cap)].clone()
+            for t in range(T):
+                place = L - T + t
+                if 0 <= place < cap:
+                    want[:, place] = new[b, :, t]
+            assert torch.equal(out[b, :, :min(L, cap)].cpu(), ref.held(want).float())
+    # reading follows the same places and leaves the dropped rows as they were
+    back = [torch.full((2, 2, T, d), -77.0, device="cuda") for _ in range(2)]
+    aq.attnq_kv4_read(st.cache, aq.AttnqKv4Seqs(st.table, lens), *back)
+    assert aq.attnq_device_status() == 6
+    there = max(0, min(T, T - over))
+    assert torch.equal(back[0][0, :, :there].cpu(), ref.held(K[0, :, :there]).float())
+    assert (back[0][0, :, there:] == -77).all() and (back[1][0, :, there:] == -77).all()
+    assert torch.equal(back[1][1].cpu(), ref.held(V[1]).float())
