@@ -748,7 +748,11 @@ __global__ void __launch_bounds__(kThreads) k_kv4_weigh_scores(const Kv4AttnPara
   const int b = blockIdx.y / p.map.Hkv, h = blockIdx.y % p.map.Hkv;
   const int L = kv4_len(p.map, b), rows = kv4_new(p.map, b) * p.G;
   const int tile0 = (int(blockIdx.x) * kWarps + warp) * kScoreTiles;
-  if (tile0 * kKv4Tile >= L) return;
+  if (tile0 * kKv4Tile >= L) {
+    // nothing to do, but the grid may not end before the kernels it depends on: the call's end is its end
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int64_t acc_at = int64_t(blockIdx.y) * p.acc_ld;
   const float4* from = p.scores + (int64_t(blockIdx.y) * (p.acc_ld / kKv4Tile) + tile0) * W + lane;
   float old[STEPS];
@@ -797,7 +801,10 @@ __global__ void __launch_bounds__(kThreads, 8) k_kv4_weigh_many(const Kv4AttnPar
   const int b = blockIdx.y / p.map.Hkv, h = blockIdx.y % p.map.Hkv;
   const int L = kv4_len(p.map, b), n = kv4_new(p.map, b), rows = n * p.G, n8 = (p.map.T * p.G + 7) >> 3;
   const int tile = int(blockIdx.x) * kWarps + warp;
-  if (int(blockIdx.x) * kWarps * kKv4Tile >= L) return;
+  if (int(blockIdx.x) * kWarps * kKv4Tile >= L) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // as above
+    return;
+  }
   const float4* from = p.scores + (int64_t(blockIdx.y) * (p.acc_ld / kKv4Tile) + tile) * n8 * 32 + lane;
   const int j0 = tile * kKv4Tile + g, j = j0 + 8 * t;  // lanes t < 2 end with token j
   const bool mine = t < 2 && j < L;

@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(128) k_kv4_join(const Kv4AttnParams p, float p
 }
 
 // Launch with programmatic stream serialisation: the kernel may start while the
-// one before it drains, and waits for it with griddepcontrol.wait.
+// one before it drains, and waits for it with griddepcontrol.wait, in every CTA and on every
+// way out: what comes next in the stream waits for this grid alone.
 template <typename... Args>
 cudaError_t kv4_launch_after(void (*kern)(Args...), dim3 grid, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg{};

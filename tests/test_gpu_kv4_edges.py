@@ -70,3 +70,28 @@ def test_append_past_the_page_table(d, over, T):
     assert torch.equal(back[0][0, :, :there].cpu(), ref.held(K[0, :, :there]).float())
     assert (back[0][0, :, there:] == -77).all() and (back[1][0, :, there:] == -77).all()
     assert torch.equal(back[1][1].cpu(), ref.held(V[1]).float())
+
+
+@pytest.mark.parametrize("T,G,pages", [(1, 4, 4), (1, 8, 4), (1, 4, 300), (9, 4, 4), (40, 8, 4)])
+def test_weights_of_an_empty_batch(T, G, pages):
+    """Sequences without tokens only: the call's last kernel has nothing to do, and still what follows in the
+    stream sees all rows written (O = 0, lse = -infinity) and no weight changed."""
+    aq = _aq()
+    B, Hkv, d, page = 600, 2, 128, 256
+    cache = aq.alloc_kv4_cache(1, page, Hkv, d)
+    table = torch.zeros((B, pages), dtype=torch.int32, device="cuda")
+    seqs = aq.AttnqKv4Seqs(table, torch.zeros(B, dtype=torch.int32, device="cuda"))
+    Q = torch.randn((B, Hkv * G, T, d), generator=torch.Generator().manual_seed(T)).to(BF16).cuda()
+    ws = torch.empty(aq.attnq_kv4_attn_workspace(cache, B, pages, Hkv * G, T), dtype=torch.uint8, device="cuda")
+    O = torch.empty_like(Q)
+    lse = torch.empty(Q.shape[:3], device="cuda")
+    acc = torch.full((B, Hkv, pages * page), -77.0, device="cuda")
+    seen = []
+    for _ in range(8):
+        O.fill_(-77.0)
+        lse.fill_(-77.0)
+        aq.attnq_kv4_attn(cache, seqs, Q, O, True, ws, lse=lse, acc_out=acc)
+        seen.append(((O != 0).any(), (lse != -math.inf).any()))
+    assert aq.attnq_device_status() == 0
+    assert not any(bool(a) or bool(b) for a, b in seen)
+    assert (acc == -77).all()
