@@ -457,8 +457,12 @@ attnq_status attnq_kv4_read(const attnq_kv4_cache* cache, const attnq_kv4_seqs* 
  * infinity in Q is recorded as ATTNQ_ENONFINITE.
  * Two calls on the same inputs give the same bits; in a batch of other lengths the order
  * in which a row's tokens are joined may differ, within these roundings.
- * workspace: DEVICE, 256-byte aligned, at least attnq_kv4_attn_workspace(...)
- * bytes (these may hold the call's scores too, 64 MB of them at the most); needs no initialisation, and calls that overlap need one each.
+ * workspace: DEVICE, 256-byte aligned; needs no initialisation, and calls that overlap need
+ * one each.  attnq_kv4_attn_workspace(...) bytes serve the call, and every call of fewer
+ * sequences, pages or query rows of the cache, at its best.  Its last min(64 MiB, B * Hkv * max_pages *
+ * page_tokens * (rows <= 4 ? 16 : 32 * ceil(rows / 8))) bytes, rows = T * Hq / Hkv, rounded up to 256,
+ * may be left out: they hold the call's scores when acc_out is given, and where they do not fit (or are
+ * more than 64 MiB) the weights are computed from K once more, slower and with other roundings.
  */
 size_t attnq_kv4_attn_workspace(const attnq_kv4_cache* cache, int32_t B, int32_t max_pages, int32_t Hq, int32_t T);
 attnq_status attnq_kv4_attn(const attnq_kv4_cache* cache, const attnq_kv4_seqs* seqs, int32_t T, int32_t Hq,

@@ -682,7 +682,7 @@ attnq_status attnq_kv4_read(const attnq_kv4_cache* cache, const attnq_kv4_seqs* 
 size_t attnq_kv4_attn_workspace(const attnq_kv4_cache* cache, int32_t B, int32_t max_pages, int32_t Hq, int32_t T) {
   if (check_kv4_shape(cache) != ATTNQ_OK || check_kv4_sizes(cache, B, max_pages, T) != ATTNQ_OK) return 0;
   if (Hq <= 0 || Hq % cache->Hkv != 0 || int64_t(Hq) * T > (int64_t(1) << 28)) return 0;
-  return kv4_attn_workspace_bytes(B, max_pages, cache->page_tokens, Hq, cache->Hkv, T, cache->d);
+  return kv4_attn_workspace_bytes(B, max_pages, cache->page_tokens, Hq, cache->Hkv, T, cache->d, true);
 }
 
 attnq_status attnq_kv4_attn(const attnq_kv4_cache* cache, const attnq_kv4_seqs* seqs, int32_t T, int32_t Hq,
@@ -700,7 +700,8 @@ attnq_status attnq_kv4_attn(const attnq_kv4_cache* cache, const attnq_kv4_seqs* 
   if (!(std::isfinite(scale) && scale > 0.0f) || (causal != 0 && causal != 1)) return ATTNQ_EINVAL;
   if (acc_in && !acc_out) return ATTNQ_EINVAL;
   if (!aligned4(lse) || !aligned4(acc_in) || !aligned4(acc_out)) return ATTNQ_EINVAL;
-  const size_t need = attnq_kv4_attn_workspace(cache, seqs->B, seqs->max_pages, Hq, T);
+  const size_t need = kv4_attn_workspace_bytes(seqs->B, seqs->max_pages, cache->page_tokens, Hq, cache->Hkv, T, cache->d,
+                                               false);
   if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return ATTNQ_EINVAL;
   int dev;
   st = device_setup(&dev);
@@ -712,7 +713,7 @@ attnq_status attnq_kv4_attn(const attnq_kv4_cache* cache, const attnq_kv4_seqs* 
   a.q_bf16 = Q->dtype == ATTNQ_BF16; a.o_bf16 = O->dtype == ATTNQ_BF16;
   a.scale = scale; a.causal = causal;
   a.lse = lse; a.acc_in = acc_in; a.acc_out = acc_out;
-  a.ws = workspace;
+  a.ws = workspace; a.ws_bytes = ws_bytes;
   const NvtxRange range("attnq_kv4_attn");
   return from_cuda(launch_kv4_attn(a, stream));
 }

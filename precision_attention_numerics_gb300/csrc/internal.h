@@ -149,8 +149,9 @@ struct Kv4AttnArgs {
   const float* acc_in;   // [B, Hkv, max_pages * page_tokens] or null (zeros)
   float* acc_out;        // null: no weights
   void* ws;
+  size_t ws_bytes;
 };
-size_t kv4_attn_workspace_bytes(int B, int max_pages, int page_tokens, int Hq, int Hkv, int T, int d);
+size_t kv4_attn_workspace_bytes(int B, int max_pages, int page_tokens, int Hq, int Hkv, int T, int d, bool with_scores);
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s);
 
 struct Kv4EvictArgs {

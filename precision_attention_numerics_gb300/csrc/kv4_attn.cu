@@ -857,11 +857,10 @@ struct Plan {
   int R, n_cta, n_rg, cl;
 };
 
-// Row groups of 8, 16 or 32 rows, and as many CTAs as the GPU holds at once (or
-// as there are chunks for their warps).
-Plan plan_of(int B, int max_tokens, int Hq, int Hkv, int T) {
+// Row groups of 8, 16, 24 or 32 of the rows of a KV head, and as many CTAs as the GPU holds at once
+// (or as there are chunks for their warps).
+Plan plan_of(int B, int max_tokens, int Hkv, int64_t rows) {
   Plan pl{};
-  const int64_t rows = int64_t(T) * (Hq / Hkv);
   pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
   const int64_t n_rg = (rows + pl.R - 1) / pl.R;
   const int64_t fill = int64_t(kKv4PlanSms) * (pl.R == 8 ? 4 : pl.R <= 16 ? 3 : 2);
@@ -898,12 +897,26 @@ size_t plan_bytes(const Plan& pl, int d) {
   return kv4_a256(rows * d * 4) + kv4_a256(rows * 8) + kv4_a256(size_t(pl.n_cta) * 16);
 }
 
-// Bytes of the scores that k_kv4_attn may leave, 0 where K is read again instead: past
-// half of the L2's 126 MB, where the scores would travel to memory and back.
+// Bytes for the parts of a call with either kernel (the output's type, which is not known here, chooses between
+// them) or with fewer rows, whose smaller groups leave room for more CTAs: a call needs no more
+// than one with more sequences, places or rows.
+size_t parts_bytes(int B, int max_tokens, int Hq, int Hkv, int T, int d) {
+  const int64_t rows = int64_t(T) * (Hq / Hkv);
+  size_t most = plan_bytes(prefill_plan(B, max_tokens, Hq, Hkv, T), d);
+  for (const int64_t n : {int64_t(8), int64_t(16), int64_t(24), int64_t(32), rows}) {
+    const size_t x = plan_bytes(plan_of(B, max_tokens, Hkv, n < rows ? n : rows), d);
+    most = x > most ? x : most;
+  }
+  return most;
+}
+
+// Bytes of the scores that k_kv4_attn leaves where there is room for them: up to half of the
+// L2's 126 MB.  Past that they would travel to memory and back, and K is read again instead.
+constexpr size_t kMaxScores = size_t(64) << 20;
 size_t scores_bytes(int B, int64_t max_tokens, int Hq, int Hkv, int T) {
-  const int64_t rows = int64_t(T) * (Hq / Hkv), most = int64_t(64) << 20;
+  const int64_t rows = int64_t(T) * (Hq / Hkv), most = int64_t(kMaxScores);
   const int64_t token = int64_t(B) * Hkv * (rows <= 4 ? 16 : (rows + 7) / 8 * 32);  // bytes of a token place
-  return token <= most / max_tokens ? size_t(token * max_tokens) : 0;
+  return token <= most / max_tokens ? size_t(token * max_tokens) : kMaxScores + 1;
 }
 
 template <int D, bool QS>
@@ -990,12 +1003,13 @@ cudaError_t run_d(const Kv4AttnParams& p, const Plan& pl, int max_tokens, cudaSt
 
 }  // namespace
 
-size_t kv4_attn_workspace_bytes(int B, int max_pages, int page_tokens, int Hq, int Hkv, int T, int d) {
-  // the output's type, which this does not know, chooses between the two
-  const size_t a = plan_bytes(plan_of(B, max_pages * page_tokens, Hq, Hkv, T), d);
-  const size_t b = plan_bytes(prefill_plan(B, max_pages * page_tokens, Hq, Hkv, T), d);
-  const size_t scores = scores_bytes(B, int64_t(max_pages) * page_tokens, Hq, Hkv, T);
-  return (a > b ? a : b) + kv4_a256(size_t(B) * Hq * T * 4) + kv4_a256(scores);
+// Without the scores this is what a call needs; with them, what serves it and every call of
+// fewer sequences, places or rows at its best.
+size_t kv4_attn_workspace_bytes(int B, int max_pages, int page_tokens, int Hq, int Hkv, int T, int d, bool with_scores) {
+  const int max_tokens = max_pages * page_tokens;
+  const size_t need = parts_bytes(B, max_tokens, Hq, Hkv, T, d) + kv4_a256(size_t(B) * Hq * T * 4);
+  const size_t scores = scores_bytes(B, max_tokens, Hq, Hkv, T);
+  return with_scores ? need + kv4_a256(scores < kMaxScores ? scores : kMaxScores) : need;
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
@@ -1003,7 +1017,7 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   const int max_tokens = kv.max_pages * kv.page_tokens;
   Plan pl = prefill_plan(kv.B, max_tokens, a.Hq, kv.Hkv, kv.T);
   const bool many = a.o_bf16 && pl.n_cta > 0;
-  if (!many) pl = plan_of(kv.B, max_tokens, a.Hq, kv.Hkv, kv.T);
+  if (!many) pl = plan_of(kv.B, max_tokens, kv.Hkv, int64_t(kv.T) * (a.Hq / kv.Hkv));
   Kv4AttnParams p{};
   p.map = kv4_map(kv);
   p.Q = a.Q;
@@ -1029,8 +1043,10 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   w += kv4_a256(rows * 8);
   p.part_seg = reinterpret_cast<int4*>(w);
   w += kv4_a256(size_t(pl.n_cta) * 16);
-  const size_t scores = many ? 0 : scores_bytes(kv.B, max_tokens, a.Hq, kv.Hkv, kv.T);
-  p.scores = a.acc_out && scores ? reinterpret_cast<float4*>(w + kv4_a256(size_t(kv.B) * a.Hq * kv.T * 4)) : nullptr;
+  uint8_t* tail = w + kv4_a256(size_t(kv.B) * a.Hq * kv.T * 4);
+  const size_t scores = scores_bytes(kv.B, max_tokens, a.Hq, kv.Hkv, kv.T);
+  const size_t room = a.ws_bytes - size_t(tail - static_cast<uint8_t*>(a.ws));
+  p.scores = a.acc_out && !many && scores <= kMaxScores && scores <= room ? reinterpret_cast<float4*>(tail) : nullptr;
   p.lse = a.lse ? a.lse : a.acc_out ? reinterpret_cast<float*>(w) : nullptr;
   p.lse_sb = int64_t(a.Hq) * kv.T;
   p.lse_sh = kv.T;

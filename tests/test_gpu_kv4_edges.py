@@ -95,3 +95,41 @@ def test_weights_of_an_empty_batch(T, G, pages):
     assert aq.attnq_device_status() == 0
     assert not any(bool(a) or bool(b) for a, b in seen)
     assert (acc == -77).all()
+
+
+@pytest.mark.parametrize("T,G,dtype", [(1, 4, BF16), (1, 8, F32), (5, 4, BF16), (40, 4, BF16), (40, 4, F32)])
+def test_workspaces_of_other_calls(T, G, dtype):
+    """The workspace of a larger call leaves the result's bits as they are (its scores are past 64 MiB, this
+    call's fit).  Without the scores' part O and lse keep their bits, and the weights come from K again: both
+    ways take fp32 sums of d products (d 2^-23 of sum |q k| scale log2 e, below 48 here), round them and the
+    row's sum a few times (2^-20 of them), so a weight moves by 2 (d 2^-23 + 2^-20) 48 < 2^-8 of itself."""
+    aq = _aq()
+    st = Setup([900, 0, 2000, 33], 2, 128, 64, dtype=dtype, seed=T + G)
+    gen = torch.Generator().manual_seed(T)
+    Q = torch.randn((4, 2 * G, T, 128), generator=gen).to(dtype).cuda()
+    start = torch.rand((4, 2, st.max_pages * 64), generator=gen).cuda()
+    rows = T * G
+    tail = min(64 << 20, 4 * 2 * st.max_pages * 64 * (16 if rows <= 4 else 32 * -(-rows // 8)))
+    own = aq.attnq_kv4_attn_workspace(st.cache, 4, st.max_pages, 2 * G, T)
+    sizes = [own, aq.attnq_kv4_attn_workspace(st.cache, 64, 9000, 2 * G, 2 * T), own - -(-tail // 256) * 256]
+    assert sizes[1] > sizes[0] > sizes[2]
+    out = []
+    for size in sizes:
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+        O, lse = torch.zeros_like(Q), torch.zeros(Q.shape[:3], device="cuda")
+        acc = torch.full_like(start, -77.0)
+        aq.attnq_kv4_attn(st.cache, aq.AttnqKv4Seqs(st.table, st.lens_t), Q, O, True, ws, lse=lse, acc_in=start,
+                          acc_out=acc)
+        assert aq.attnq_device_status() == 0
+        out.append((O, lse, acc))
+    for x, y in zip(out[0], out[1]):
+        assert torch.equal(x, y)
+    assert torch.equal(out[0][0], out[2][0]) and torch.equal(out[0][1], out[2][1])
+    for b, L in enumerate(st.lens):
+        a, c = (out[i][2][b, :, :L] - start[b, :, :L] for i in (0, 2))
+        tol = 2.0 ** -8 * a.abs() + 2.0 ** -23 * (start[b, :, :L] + rows) * 2
+        assert ((a - c).abs() <= tol).all()
+        assert (out[2][2][b, :, L:] == -77).all()
+    with pytest.raises(aq.AttnqError):
+        aq.attnq_kv4_attn(st.cache, aq.AttnqKv4Seqs(st.table, st.lens_t), Q, O, True,
+                          torch.empty(sizes[2] - 1, dtype=torch.uint8, device="cuda"))

@@ -195,3 +195,39 @@ def test_no_calls_in_the_kernel_that_moves_registers(tmp_path):
     assert r.returncode == 0, r.stderr
     functions = [l for l in r.stderr.splitlines() if "Function properties for" in l]
     assert functions and all("k_kv4_prefill" in f or "k_kv4_join" in f for f in functions), functions
+
+
+def test_attention_workspace_grows_with_the_call(aq):
+    """A buffer for the largest call serves every smaller one, and what a call must have is that less the scores."""
+    mk = lambda **k: aq.AttnqKv4Cache(**{**dict(num_pages=10, page_tokens=64, Hkv=8, d=128), **k})
+    for cache in (mk(), mk(Hkv=1, d=64), mk(Hkv=3, page_tokens=16)):
+        for G in (1, 3, 4, 7):
+            size = lambda B, pages, T, G=G: aq.attnq_kv4_attn_workspace(cache, B, pages, G * cache.Hkv, T)
+            for B, pages, T in ((8, 512, 1), (16, 512, 1), (1, 8, 5), (2, 40, 9), (300, 4, 2)):
+                last = 0
+                for t in (1, 2, 3, 4, 5, 6, 8, 9, 16, 17, 24, 25, 32, 33, 64, 65, 100, 257, 1024):
+                    assert size(B, pages, t) >= last, (B, pages, t, G)
+                    last = size(B, pages, t)
+                last = 0
+                for b in (1, 2, 3, 5, 8, 16, 17, 40, 100, 300, 1000, 5000):
+                    assert size(b, pages, T) >= last, (b, pages, T, G)
+                    last = size(b, pages, T)
+                last = 0
+                for n in (1, 2, 3, 7, 8, 20, 64, 100, 512, 513, 1024, 2048, 5000, 100000):
+                    assert size(B, n, T) >= last, (B, n, T, G)
+                    last = size(B, n, T)
+            last = 0
+            for g in range(1, 40):
+                assert size(8, 512, 1, G=g) >= last
+                last = size(8, 512, 1, G=g)
+    # the least that a call takes, as attnq.h states it: a byte less is refused (on the host)
+    L = aq.load_library()
+    for B, pages, Hq, T in ((2, 4, 4, 1), (2, 4, 4, 3), (2, 1 << 20, 4, 1), (2, 4, 64, 40)):
+        c, s = _cache(aq), _seqs(aq, B=B, max_pages=pages)
+        q, o = _rows(aq, H=Hq, T=T), _rows(aq, H=Hq, T=T, data=FAKE + (1 << 24))
+        rows = T * Hq // 2
+        tail = min(64 << 20, B * 2 * pages * 16 * (16 if rows <= 4 else 32 * -(-rows // 8)))
+        least = L.attnq_kv4_attn_workspace(C.byref(c), B, pages, Hq, T) - -(-tail // 256) * 256
+        assert least > 0
+        assert L.attnq_kv4_attn(C.byref(c), C.byref(s), T, Hq, C.byref(q), C.byref(o), C.c_float(0.125), 1, None, None,
+                                None, FAKE, least - 1, None) == 1
