@@ -633,8 +633,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_kv4_weights(const Kv4AttnParams
         const int row = row0 + i;
         float bias = -INFINITY;  // rows that are not there, or see nothing, weigh nothing
         if (row < rows) {
-          const float l = p.lse[sg.b * p.lse_sb + (sg.h * p.G + row % p.G) * p.lse_sh + row / p.G];
-          if (l != -INFINITY) bias = -l * 1.4426950408889634f;
+          const float l = p.lse2[sg.b * p.lse_sb + (sg.h * p.G + row % p.G) * p.lse_sh + row / p.G];
+          if (l != -INFINITY) bias = -l;
         }
         s_bias[i] = bias;
       }
@@ -738,8 +738,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_kv4_weights(const Kv4AttnParams
 // The same from the scores that k_kv4_attn has left: their bytes are read instead of K turned into operands
 // and multiplied again.  With up to 8 rows a warp takes eight tiles, W lanes (16 for up to 4 rows,
 // else 32) to a tile: 8 x 16384 tokens of 32 heads on 8 take 9 us (2 of them for the stores in
-// k_kv4_attn), where reading K again took 31.  acc_in and the lengths are read
-// before the wait for the kernels before: none of this call's writes them.
+// k_kv4_attn), where reading K again took 31.  The kept scores have been rounded to fp32 (c s, log2 units, as
+// the rows' maxima and log-sums are), where the kernel above has one fma: 2^-24 of the score.
+// acc_in and the lengths are read before the wait for the kernels before: none of this call's writes them.
 constexpr int kScoreTiles = 8;
 template <int W>
 __global__ void __launch_bounds__(kThreads) k_kv4_weigh_scores(const Kv4AttnParams p) {
@@ -771,9 +772,9 @@ __global__ void __launch_bounds__(kThreads) k_kv4_weigh_scores(const Kv4AttnPara
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int row = 2 * t + x;
-    const float l = row < rows ? p.lse[b * p.lse_sb + (h * p.G + row % p.G) * p.lse_sh + row / p.G] : -INFINITY;
+    const float l = row < rows ? p.lse2[b * p.lse_sb + (h * p.G + row % p.G) * p.lse_sh + row / p.G] : -INFINITY;
     live[x] = l != -INFINITY;  // rows that are not there, or see nothing, weigh nothing
-    bias[x] = -l * 1.4426950408889634f;
+    bias[x] = -l;
   }
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
@@ -820,8 +821,8 @@ __global__ void __launch_bounds__(kThreads, 8) k_kv4_weigh_many(const Kv4AttnPar
       float bias = 0.0f;
       int lim = 0;  // rows that are not there, or see nothing, weigh nothing
       if (row < rows) {
-        const float l = p.lse[b * p.lse_sb + (h * p.G + row % p.G) * p.lse_sh + row / p.G];
-        bias = -l * 1.4426950408889634f;
+        const float l = p.lse2[b * p.lse_sb + (h * p.G + row % p.G) * p.lse_sh + row / p.G];
+        bias = -l;
         if (l != -INFINITY) lim = p.causal ? min(max(L - n + row / p.G + 1, 0), L) : L;
       }
       s_bias[i] = bias;
@@ -991,7 +992,7 @@ template <int D>
 cudaError_t run_d(const Kv4AttnParams& p, const Plan& pl, int max_tokens, cudaStream_t s) {
   if (pl.R == kKv4PrefillRows) {
     const bool inexact = !p.q_bf16 || p.signs;  // queries that one fp16 term rounds
-    cudaError_t e = launch_kv4_prefill(p, D, inexact && p.lse, s);
+    cudaError_t e = launch_kv4_prefill(p, D, inexact && (p.lse || p.acc_out), s);
     if (e != cudaSuccess || !p.acc_out) return e;
     return inexact ? run_weights<D, true>(p, max_tokens, s) : run_weights<D, false>(p, max_tokens, s);
   }
@@ -1047,7 +1048,8 @@ cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t s) {
   const size_t scores = scores_bytes(kv.B, max_tokens, a.Hq, kv.Hkv, kv.T);
   const size_t room = a.ws_bytes - size_t(tail - static_cast<uint8_t*>(a.ws));
   p.scores = a.acc_out && !many && scores <= kMaxScores && scores <= room ? reinterpret_cast<float4*>(tail) : nullptr;
-  p.lse = a.lse ? a.lse : a.acc_out ? reinterpret_cast<float*>(w) : nullptr;
+  p.lse = a.lse;
+  p.lse2 = a.acc_out ? reinterpret_cast<float*>(w) : nullptr;
   p.lse_sb = int64_t(a.Hq) * kv.T;
   p.lse_sh = kv.T;
   p.acc_in = a.acc_in;

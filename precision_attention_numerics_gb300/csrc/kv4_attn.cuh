@@ -24,7 +24,8 @@ struct Kv4AttnParams {
   const float* v_scale;
   float inv_sqrt_d;
   float scale_log2e;
-  float* lse;
+  float* lse;      // ln of the rows' sums, or null
+  float* lse2;     // log2 of them for the weights (as ln they would be rounded twice more), null without weights
   int64_t lse_sb, lse_sh;
   int n_cta;       // CTAs the chunks are dealt to
   int ov;          // what beginning a segment costs, in chunks
@@ -239,6 +240,14 @@ struct Kv4Line {
   }
 };
 
+// The log-sum of a row of maximum mx (log2 units) and sum l, which holds 2^p_bits; -infinity when it saw no token.
+__device__ __forceinline__ void kv4_write_lse(const Kv4AttnParams& p, int64_t at, float mx, float l, float p_bits) {
+  if (!p.lse && !p.lse2) return;
+  const float l2 = l > 0.0f ? mx + (log2f(l) - p_bits) : -INFINITY;
+  if (p.lse) p.lse[at] = l2 * 0.69314718055994531f;
+  if (p.lse2) p.lse2[at] = l2;
+}
+
 // Row `row` of (b, h): O = g_v x / l (0 when the row saw no token) and lse.
 template <int D>
 __device__ __forceinline__ void kv4_write_row(const Kv4AttnParams& p, int b, int h, int row, int lane, float mx, float l,
@@ -256,9 +265,7 @@ __device__ __forceinline__ void kv4_write_row(const Kv4AttnParams& p, int b, int
     else
       reinterpret_cast<float2*>(dst)[(lane * E + e) / 2] = make_float2(x[e] * inv, x[e + 1] * inv);
   }
-  if (p.lse && lane == 0)
-    p.lse[b * p.lse_sb + head * p.lse_sh + t] =
-        l > 0.0f ? (mx + (log2f(l) - p_bits)) * 0.69314718055994531f : -INFINITY;
+  if (lane == 0) kv4_write_lse(p, b * p.lse_sb + head * p.lse_sh + t, mx, l, p_bits);
 }
 
 // Joins the parts of a segment that several CTAs had, in their order: block

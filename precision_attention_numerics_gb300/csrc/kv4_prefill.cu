@@ -598,9 +598,7 @@ __device__ __forceinline__ void softmax_rows(const Kv4AttnParams& p, Kv4Line<kPr
       }
       if (live && half == 0) {
         if (!entire) p.part_ml[to] = make_float2(m[w], l[w]);
-        else if (p.lse)
-          p.lse[sg.b * p.lse_sb + head * p.lse_sh + tq] =
-              l[w] > 0.0f ? (m[w] + (log2f(l[w]) - kPreBits)) * 0.69314718055994531f : -INFINITY;
+        else kv4_write_lse(p, sg.b * p.lse_sb + head * p.lse_sh + tq, m[w], l[w], kPreBits);
       }
     }
     const int4 record = sg.record(p, c1, slot);

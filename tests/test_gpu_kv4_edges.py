@@ -133,3 +133,37 @@ def test_workspaces_of_other_calls(T, G, dtype):
     with pytest.raises(aq.AttnqError):
         aq.attnq_kv4_attn(st.cache, aq.AttnqKv4Seqs(st.table, st.lens_t), Q, O, True,
                           torch.empty(sizes[2] - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("T,pages", [(1, 1), (5, 1), (16, 1), (16, 9000), (40, 1)])
+@pytest.mark.parametrize("size", [3.0, 40.0, 700.0])
+def test_weight_of_an_only_token(T, pages, size):
+    """A sequence of one token gives it the weight 1, however large the score.
+
+    In log2 units let y = s c be the score, m its fp32 value and u its last place.  The exponent
+    fma(s, c, 15 - m) is exact to 2^-21 (for m > 16 15 - m is a multiple of u that fp32 holds), so
+    m + (log2 l - 15), rounded to fp32, is within u / 2 + 2^-18 of y (2^-18: an fp32 near 15, ex2, log2).  The
+    weight's exponent is y or m less that: at most u + 2^-18, times ln 2 < 0.7.  Both come from the same raw
+    sum s, but for T = 40, where tcgen05 adds the d products in another order: d 2^-23 of
+    sum |q k| (= y here, q lies along k) on either side."""
+    aq = _aq()
+    B, d = 320, 64
+    st = Setup([1] * B, 1, d, 16, dtype=F32, seed=T)
+    gen = torch.Generator().manual_seed(int(size) + T)
+    k = torch.stack([st.held(b, 0)[0][0] for b in range(B)])
+    want = size * (1 + torch.rand((B, 1), generator=gen).double())
+    Q = torch.zeros((B, 1, T, d))
+    Q[:, 0, 0] = (want / math.log2(math.e) / 0.125 / (k * k).sum(-1, keepdim=True) * k).float()
+    y = (Q[:, 0, 0].double() * k).sum(-1) * 0.125 * math.log2(math.e)
+    table = torch.full((B, max(pages, st.max_pages)), -1, dtype=torch.int32, device="cuda")
+    table[:, :st.max_pages] = st.table
+    one = torch.ones(B, dtype=torch.int32, device="cuda")  # row 0 alone exists, whatever T
+    acc = torch.zeros((B, 1, table.shape[1] * 16), device="cuda")
+    ws = torch.empty(aq.attnq_kv4_attn_workspace(st.cache, B, table.shape[1], 1, T), dtype=torch.uint8, device="cuda")
+    O = torch.empty((B, 1, T, d), device="cuda", dtype=BF16 if T == 40 else F32)
+    aq.attnq_kv4_attn(st.cache, aq.AttnqKv4Seqs(table, st.lens_t, one), Q.cuda(), O, True, ws, acc_out=acc)
+    assert aq.attnq_device_status() == 0
+    u = torch.exp2(torch.floor(torch.log2(y)) - 23)
+    tol = 0.7 * (u + 2.0 ** -18 + (2 * d * 2.0 ** -23 * y if T == 40 else 0.0))
+    off = (acc[:, 0, 0].cpu().double() - 1).abs()
+    assert (off <= tol).all(), (off / tol).max()
