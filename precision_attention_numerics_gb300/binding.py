@@ -360,6 +360,16 @@ def _refuse(what: str):
     raise AttnqError(1, what)
 
 
+def _int32(*values) -> bool:
+    """Whether a call's int32 arguments can hold these (ctypes cuts longer ones off in silence)."""
+    return -(1 << 31) <= min(values) and max(values) < 1 << 31
+
+
+def _kv4_sizes(cache: AttnqKv4Cache) -> Optional[_Kv4Cache]:
+    """The cache's struct for the functions that ask for bytes; None (0 bytes) where its sizes do not fit."""
+    return cache._c() if _int32(cache.num_pages, cache.page_tokens, cache.Hkv, cache.d) else None
+
+
 def _kv4_ptr(t, what: str, name: str, dtype, dev: int, shape=None) -> int:
     """Address of a contiguous tensor of device `dev`, of the given type and shape."""
     if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (shape is not None and
@@ -376,18 +386,21 @@ def _kv4_structs(what: str, cache: AttnqKv4Cache, seqs: AttnqKv4Seqs, dev: int):
     pages, signs, gk, gv = cache.pages, cache.signs, cache.k_scale, cache.v_scale
     if pages is None or pages.numel() < cache.num_pages * cache.page_tokens * Hkv * (d + d // 8):
         _refuse(f"{what}: the cache has fewer than attnq_kv4_cache_bytes(cache) bytes of pages")
-    c = _pack_kv4_cache(cache.num_pages, cache.page_tokens, Hkv, d, cache.flags,
-                        0 if signs is None else _kv4_ptr(signs, what, "signs", torch.int8, dev, (d,)),
-                        0 if gk is None else _kv4_ptr(gk, what, "k_scale", torch.float32, dev, (Hkv,)),
-                        0 if gv is None else _kv4_ptr(gv, what, "v_scale", torch.float32, dev, (Hkv,)),
-                        _kv4_ptr(pages, what, "pages", torch.uint8, dev))
     table, new_lens = seqs.table, seqs.new_lens
     if table.dim() != 2:
         _refuse(f"{what}: table must be [B, max_pages]")
     B, max_pages = table.shape
-    s = _pack_kv4_seqs(B, max_pages, _kv4_ptr(table, what, "table", torch.int32, dev),
-                       _kv4_ptr(seqs.lens, what, "lens", torch.int32, dev, (B,)),
-                       0 if new_lens is None else _kv4_ptr(new_lens, what, "new_lens", torch.int32, dev, (B,)))
+    try:
+        c = _pack_kv4_cache(cache.num_pages, cache.page_tokens, Hkv, d, cache.flags,
+                            0 if signs is None else _kv4_ptr(signs, what, "signs", torch.int8, dev, (d,)),
+                            0 if gk is None else _kv4_ptr(gk, what, "k_scale", torch.float32, dev, (Hkv,)),
+                            0 if gv is None else _kv4_ptr(gv, what, "v_scale", torch.float32, dev, (Hkv,)),
+                            _kv4_ptr(pages, what, "pages", torch.uint8, dev))
+        s = _pack_kv4_seqs(B, max_pages, _kv4_ptr(table, what, "table", torch.int32, dev),
+                           _kv4_ptr(seqs.lens, what, "lens", torch.int32, dev, (B,)),
+                           0 if new_lens is None else _kv4_ptr(new_lens, what, "new_lens", torch.int32, dev, (B,)))
+    except struct.error:  # a size that 32 bits do not hold
+        _refuse(f"{what}: a size of the cache or the table")
     return c, s, B, max_pages
 
 
@@ -401,7 +414,7 @@ def _kv4_rows(t, what: str, name: str, dev: int, B: int, H: int, T: int, d: int)
         code = ATTNQ_F32
     else:
         _refuse(f"{what}: {name} must be bfloat16 or float32")
-    if t.get_device() != dev or t.shape != (B, H, T, d) or stride[3] != 1:
+    if t.get_device() != dev or t.shape != (B, H, T, d) or stride[3] != 1 or H >> 31 or T >> 31:
         _refuse(f"{what}: {name} must be [{B}, {H}, {T}, {d}] on the current CUDA device, its last axis contiguous")
     return _pack_rows(t.data_ptr(), code, stride[0], stride[1], stride[2])
 
@@ -421,8 +434,8 @@ def _kv4_stream(stream, dev: int):
 
 
 def attnq_kv4_cache_bytes(cache: AttnqKv4Cache) -> int:
-    c = cache._c()
-    return int(load_library().attnq_kv4_cache_bytes(C.byref(c)))
+    c = _kv4_sizes(cache)
+    return int(load_library().attnq_kv4_cache_bytes(C.byref(c))) if c is not None else 0
 
 
 def _kv4_rows_call(fn, what: str, cache, seqs, K, V, names, k_mean, stream) -> None:
@@ -454,8 +467,10 @@ def attnq_kv4_read(cache: AttnqKv4Cache, seqs: AttnqKv4Seqs, K_out, V_out, strea
 
 
 def attnq_kv4_attn_workspace(cache: AttnqKv4Cache, B: int, max_pages: int, Hq: int, T: int) -> int:
-    c = cache._c()
-    return int(load_library().attnq_kv4_attn_workspace(C.byref(c), int(B), int(max_pages), int(Hq), int(T)))
+    c, B, max_pages, Hq, T = _kv4_sizes(cache), int(B), int(max_pages), int(Hq), int(T)
+    if c is None or not _int32(B, max_pages, Hq, T):
+        return 0
+    return int(load_library().attnq_kv4_attn_workspace(C.byref(c), B, max_pages, Hq, T))
 
 
 def attnq_kv4_attn(cache: AttnqKv4Cache, seqs: AttnqKv4Seqs, Q, O, causal: bool, workspace, scale=None, lse=None,
@@ -486,8 +501,10 @@ def attnq_kv4_attn(cache: AttnqKv4Cache, seqs: AttnqKv4Seqs, Q, O, causal: bool,
 
 
 def attnq_kv4_evict_workspace(cache: AttnqKv4Cache, B: int, max_pages: int, budget: int) -> int:
-    c = cache._c()
-    return int(load_library().attnq_kv4_evict_workspace(C.byref(c), int(B), int(max_pages), int(budget)))
+    c, B, max_pages, budget = _kv4_sizes(cache), int(B), int(max_pages), int(budget)
+    if c is None or not _int32(B, max_pages, budget):
+        return 0
+    return int(load_library().attnq_kv4_evict_workspace(C.byref(c), B, max_pages, budget))
 
 
 def attnq_kv4_evict(cache: AttnqKv4Cache, seqs: AttnqKv4Seqs, acc, budget: int, n_sink: int, n_recent: int,
@@ -502,10 +519,12 @@ def attnq_kv4_evict(cache: AttnqKv4Cache, seqs: AttnqKv4Seqs, acc, budget: int, 
     Hkv, page, f32, i32, budget = cache.Hkv, cache.page_tokens, torch.float32, torch.int32, int(budget)
     if dst_table.dim() != 2 or dst_table.shape[0] != B:
         _refuse(f"{what}: dst_table must be [B, dst_pages]")
-    dst_pages = dst_table.shape[1]
+    dst_pages, n_sink, n_recent = dst_table.shape[1], int(n_sink), int(n_recent)
+    if not _int32(budget, n_sink, n_recent, dst_pages):
+        _refuse(f"{what}: budget, n_sink, n_recent or dst_pages")
     _check(load_library().attnq_kv4_evict(
         c, s, _kv4_ptr(acc, what, "acc", f32, dev, (B, Hkv, max_pages * page)), budget,
-        int(n_sink), int(n_recent), _kv4_ptr(dst_table, what, "dst_table", i32, dev), dst_pages,
+        n_sink, n_recent, _kv4_ptr(dst_table, what, "dst_table", i32, dev), dst_pages,
         _kv4_ptr(new_lens, what, "new_lens", i32, dev, (B,)), _kv4_ptr(kept, what, "kept", i32, dev, (B, Hkv, budget)),
         None if acc_out is None else _kv4_ptr(acc_out, what, "acc_out", f32, dev, (B, Hkv, dst_pages * page)),
         _kv4_ptr(workspace, what, "workspace", workspace.dtype, dev), workspace.nbytes, _kv4_stream(stream, dev)), what)

@@ -167,3 +167,32 @@ def test_weight_of_an_only_token(T, pages, size):
     tol = 0.7 * (u + 2.0 ** -18 + (2 * d * 2.0 ** -23 * y if T == 40 else 0.0))
     off = (acc[:, 0, 0].cpu().double() - 1).abs()
     assert (off <= tol).all(), (off / tol).max()
+
+
+def test_binding_refuses_what_32_bits_do_not_hold():
+    """Numbers past 32 bits would reach the library cut off: 2^32 + 1 rows as one, 2^32 sinks as none."""
+    aq = _aq()
+    st = Setup([40], 1, 64, 16, seed=3, spare=10)
+    w = 1 << 32
+    one = torch.zeros((1, 1, 1, 64), dtype=BF16, device="cuda")
+    many = one.expand(1, 1, w + 1, 64)
+    before = st.cache.pages.clone()
+    with pytest.raises(aq.AttnqError):
+        aq.attnq_kv4_append(st.cache, aq.AttnqKv4Seqs(st.table, st.lens_t), many, many)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    with pytest.raises(aq.AttnqError):
+        aq.attnq_kv4_attn(st.cache, aq.AttnqKv4Seqs(st.table, st.lens_t), many, many, True, ws)
+    big = aq.AttnqKv4Cache(st.cache.num_pages + w, 16, 1, 64, 0, None, None, None, st.cache.pages)
+    with pytest.raises(aq.AttnqError):
+        aq.attnq_kv4_append(big, aq.AttnqKv4Seqs(st.table, st.lens_t), one, one)
+    used = set(st.table.flatten().tolist())
+    dst = torch.tensor([[p for p in range(st.cache.num_pages) if p not in used][0]], dtype=torch.int32, device="cuda")
+    acc = torch.rand((1, 1, st.max_pages * 16), device="cuda")
+    new = torch.full((1,), -5, dtype=torch.int32, device="cuda")
+    kept = torch.full((1, 1, 16), -5, dtype=torch.int32, device="cuda")
+    for sink, recent in ((w, 4), (4, w), (w + 2, 4), (4, w + 2)):
+        with pytest.raises(aq.AttnqError):
+            aq.attnq_kv4_evict(st.cache, aq.AttnqKv4Seqs(st.table, st.lens_t), acc, 16, sink, recent, dst, new, kept, None,
+                               ws)
+    assert aq.attnq_device_status() == 0
+    assert new.item() == -5 and (kept == -5).all() and torch.equal(before, st.cache.pages)

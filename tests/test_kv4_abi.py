@@ -231,3 +231,23 @@ def test_attention_workspace_grows_with_the_call(aq):
         assert least > 0
         assert L.attnq_kv4_attn(C.byref(c), C.byref(s), T, Hq, C.byref(q), C.byref(o), C.c_float(0.125), 1, None, None,
                                 None, FAKE, least - 1, None) == 1
+
+
+def test_sizes_past_32_bits_are_not_cut_off(aq):
+    mk = lambda **k: aq.AttnqKv4Cache(**{**dict(num_pages=10, page_tokens=64, Hkv=8, d=128), **k})
+    w = 1 << 32
+    for bad in (dict(num_pages=w + 10), dict(page_tokens=w + 64), dict(Hkv=w + 8), dict(d=w + 128)):
+        assert aq.attnq_kv4_cache_bytes(mk(**bad)) == 0
+        assert aq.attnq_kv4_attn_workspace(mk(**bad), 1, 1, 8, 1) == 0
+        assert aq.attnq_kv4_evict_workspace(mk(**bad), 1, 1, 1) == 0
+        with pytest.raises(aq.AttnqError):
+            aq.alloc_kv4_cache(**{**dict(num_pages=10, page_tokens=64, Hkv=8, d=128), **bad}, device="cpu")
+    for i in range(4):
+        sizes = [1, 1, 8, 1]
+        assert aq.attnq_kv4_attn_workspace(mk(), *sizes) > 0
+        sizes[i] += w
+        assert aq.attnq_kv4_attn_workspace(mk(), *sizes) == 0
+    for i in range(3):
+        sizes = [1, 1, 1]
+        sizes[i] += w
+        assert aq.attnq_kv4_evict_workspace(mk(), *sizes) == 0
