@@ -721,7 +721,7 @@ attnq_status attnq_kv4_attn(const attnq_kv4_cache* cache, const attnq_kv4_seqs* 
 size_t attnq_kv4_evict_workspace(const attnq_kv4_cache* cache, int32_t B, int32_t max_pages, int32_t budget) {
   if (check_kv4_shape(cache) != ATTNQ_OK || check_kv4_sizes(cache, B, max_pages, 1) != ATTNQ_OK || budget <= 0)
     return 0;
-  return kv4_evict_workspace_bytes(B, cache->Hkv, max_pages * cache->page_tokens, budget);
+  return 256;  // reserved: the selection works in shared memory and in the outputs
 }
 
 attnq_status attnq_kv4_evict(const attnq_kv4_cache* cache, const attnq_kv4_seqs* seqs, const float* acc,
@@ -748,7 +748,6 @@ attnq_status attnq_kv4_evict(const attnq_kv4_cache* cache, const attnq_kv4_seqs*
   a.budget = budget; a.n_sink = n_sink; a.n_recent = n_recent;
   a.dst_table = dst_table; a.dst_pages = dst_pages;
   a.new_lens = new_lens; a.kept = kept; a.acc_out = acc_out;
-  a.ws = workspace;
   const NvtxRange range("attnq_kv4_evict");
   return from_cuda(launch_kv4_evict(a, stream));
 }

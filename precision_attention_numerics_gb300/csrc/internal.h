@@ -163,9 +163,7 @@ struct Kv4EvictArgs {
   int32_t* new_lens;     // [B]
   int32_t* kept;         // [B, Hkv, budget]
   float* acc_out;        // [B, Hkv, dst_pages * page_tokens] or null
-  void* ws;
 };
-size_t kv4_evict_workspace_bytes(int B, int Hkv, int max_tokens, int budget);
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s);
 
 // ---- driver entry point for tensor maps ------------------------------------

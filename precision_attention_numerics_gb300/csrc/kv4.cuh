@@ -197,64 +197,6 @@ __device__ __forceinline__ void kv4_v_frag(uint32_t w, uint32_t s01, uint32_t s8
   a[3] = hmul2_u(a[3], s89);
 }
 
-// One row of d elements, D / 32 consecutive ones per lane, as floats.
-template <int D, bool BF16>
-__device__ __forceinline__ void kv4_load_row(const void* row, int lane, float (&x)[D / 32]) {
-  if constexpr (BF16) {
-    if constexpr (D == 128) {
-      const uint2 v = __ldg(static_cast<const uint2*>(row) + lane);
-      x[0] = __uint_as_float(v.x << 16);
-      x[1] = __uint_as_float(v.x & 0xFFFF0000u);
-      x[2] = __uint_as_float(v.y << 16);
-      x[3] = __uint_as_float(v.y & 0xFFFF0000u);
-    } else {
-      const uint32_t v = __ldg(static_cast<const uint32_t*>(row) + lane);
-      x[0] = __uint_as_float(v << 16);
-      x[1] = __uint_as_float(v & 0xFFFF0000u);
-    }
-  } else {
-    if constexpr (D == 128) {
-      const float4 v = __ldg(static_cast<const float4*>(row) + lane);
-      x[0] = v.x;
-      x[1] = v.y;
-      x[2] = v.z;
-      x[3] = v.w;
-    } else {
-      const float2 v = __ldg(static_cast<const float2*>(row) + lane);
-      x[0] = v.x;
-      x[1] = v.y;
-    }
-  }
-}
-
-// x <- (signs * x) H / sqrt(d), the row spread over the warp as above:
-// butterflies of stride 1, 2, ..., d / 2 (the first ones inside a lane), then
-// one multiplication by fl32(1 / sqrt d).
-template <int D>
-__device__ __forceinline__ void kv4_rotate(float (&x)[D / 32], const int8_t* signs, int lane, float inv_sqrt_d) {
-  constexpr int E = D / 32;
-#pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = __fmul_rn(x[i], float(signs[lane * E + i]));
-#pragma unroll
-  for (int h = 1; h < E; h *= 2)
-#pragma unroll
-    for (int i = 0; i < E; ++i)
-      if (!(i & h)) {
-        const float a = x[i], b = x[i + h];
-        x[i] = __fadd_rn(a, b);
-        x[i + h] = __fsub_rn(a, b);
-      }
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2)
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float y = __shfl_xor_sync(0xffffffffu, x[i], o);
-      x[i] = (lane & o) ? __fsub_rn(y, x[i]) : __fadd_rn(x[i], y);
-    }
-#pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = __fmul_rn(x[i], inv_sqrt_d);
-}
-
 // Sixteen consecutive elements as floats.
 template <bool BF16>
 __device__ __forceinline__ void kv4_load16(const void* src, float (&x)[16]) {
@@ -278,8 +220,9 @@ __device__ __forceinline__ void kv4_load16(const void* src, float (&x)[16]) {
   }
 }
 
-// (signs * x) H / sqrt(d) with the row's blocks on d / 16 neighbouring lanes:
-// the butterflies of kv4_rotate, in the same order.
+// x <- (signs * x) H / sqrt(d), the row's blocks on d / 16 neighbouring lanes:
+// butterflies of stride 1, 2, ..., d / 2 (the first four inside a lane), then
+// one multiplication by fl32(1 / sqrt d).
 template <int D>
 __device__ __forceinline__ void kv4_rotate16(float (&x)[16], const int8_t* signs, int blk, float inv_sqrt_d) {
   const uint4 sg = __ldg(reinterpret_cast<const uint4*>(signs) + blk);

@@ -356,8 +356,6 @@ __global__ void __launch_bounds__(128) k_kv4_gather(const EvictParams p, const K
 
 }  // namespace
 
-size_t kv4_evict_workspace_bytes(int, int, int, int) { return 256; }
-
 cudaError_t launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t s) {
   EvictParams p{};
   p.map = kv4_map(a.kv);

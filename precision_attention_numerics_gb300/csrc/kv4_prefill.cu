@@ -193,8 +193,8 @@ __device__ __forceinline__ void make_tiles(const Kv4AttnParams& p, Kv4Line<kPre,
             stmatrix4(dst + uint32_t(q) * uint32_t(kTok * 128) + (swz ^ (uint32_t(x) << 5)), a);
           }
         }
-        // the ring of four flags outlives their readers: the softmax of this chunk is
-        // done before the S product that frees this stage two chunks on
+        // the ring of four flags outlives its readers: S of the next chunk is issued when the softmax of this one
+        // has handed P over, and it has to be done before K of the chunk after that is made here
         if (lane == 0) s_there[(i & 3u) * 8 + tile] = there;
       }
       fence_proxy_async_smem();
