@@ -448,12 +448,15 @@ attnq_status attnq_kv4_read(const attnq_kv4_cache* cache, const attnq_kv4_seqs* 
  * softmax weight; acc_in NULL counts as zeros and may equal acc_out; places from
  * lens[b] on are left as they were.  The result does not depend on timing: no
  * atomics, and a fixed order of every sum.
- * Softmax statistics, sums and accumulators are fp32.  The held K and V (without
- * k_scale and v_scale) are exact in fp16, and so is a bf16 query up to a power of
- * two; rotated or fp32 queries enter the first product as two fp16 terms (22 bits), or
+ * Softmax statistics, sums and accumulators are fp32.  The held K and V (without k_scale and
+ * v_scale) are exact in fp16, and a row of Q is scaled by a power of two into fp16's range, where no element
+ * is off by more than 2^-39 of the row's largest beside what follows.  A bf16 query loses no bits; rotated
+ * or fp32 queries enter the first product as two fp16 terms (22 bits), or
  * as one (11 bits) where O is bf16, neither lse nor acc_out is given and more than 32 rows
- * (T * Hq / Hkv) share a KV head.  The softmax weights enter the second product in
- * fp16 (two fp16 terms for fp32 O).  Scores past the fp32 range are unspecified.  A NaN or an
+ * (T * Hq / Hkv) share a KV head: a caller that wants both terms there asks for lse.  The softmax weights
+ * enter the second product in fp16 (two fp16 terms for fp32 O), with a step of 2^-39 of the weight of the row's
+ * largest score, or of 2^-31 where O is bf16 and more than 32 rows share a KV head; smaller ones are lost
+ * to O, not to lse.  Scores past the fp32 range are unspecified.  A NaN or an
  * infinity in Q is recorded as ATTNQ_ENONFINITE.
  * Two calls on the same inputs give the same bits; in a batch of other lengths the order
  * in which a row's tokens are joined may differ, within these roundings.

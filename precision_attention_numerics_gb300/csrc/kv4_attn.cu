@@ -13,9 +13,9 @@
 // operands of both in register order.  P goes from accumulator to B operand
 // with movmatrix, inside the warp.
 //
-// Precision: K, V and unrotated bf16 queries are exact in fp16; rotated or fp32
-// queries are split into two halves (hi + lo, 22 bits; QS), the second product
-// added in the same accumulators.  P is rounded to fp16 (2^-11 relative, an eighth of
+// Precision: K and V are exact in fp16, and unrotated bf16 queries down to 2^-31 of their row's largest
+// element (within 2^-39 of it below); rotated or fp32 queries are split into two halves (hi + lo, 22 bits, the
+// same 2^-39 at the least; QS), the second product added in the same accumulators.  P is rounded to fp16 (2^-11 relative, an eighth of
 // the bf16 output's rounding) for bf16 outputs and split in two for fp32 outputs
 // (PS).  Scores, maxima, sums and outputs are fp32.
 #include <cfloat>
@@ -91,7 +91,7 @@ __device__ __forceinline__ void load_queries(const Kv4AttnParams& p, int b, int 
       if (blk == 0) {
         const bool live = row < n * p.G;
         // at least the smallest normal number: a masked score, -infinity, times 0 would be NaN, and
-        // |s| < 2^20, so the products below it are nothing beside 1 either way
+        // |s| < 2^34, so the products below it are nothing beside 1 either way
         c[i] = fmaxf(live ? p.scale_log2e * gk * norm : 0.0f, FLT_MIN);
         lim[i] = live ? (p.causal ? min(max(L - n + row / p.G + 1, 0), L) : L) : 0x7FFFFFFF;
         if constexpr (PAIR) {

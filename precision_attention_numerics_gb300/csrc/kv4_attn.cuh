@@ -75,8 +75,11 @@ __device__ __forceinline__ void kv4_unpack16(const Kv4Raw16& r, bool bf16, float
     for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]);
   }
 }
-// Rotates the row (on d / 16 neighbouring lanes) and returns 2^-e for 2^e <= its largest magnitude <
-// 2^(e + 1), the exponent held to what both powers can express; norm = 2^e.
+// Rotates the row (on d / 16 neighbouring lanes) and returns 2^(14 - e) for 2^e <= its largest magnitude <
+// 2^(e + 1); norm = 2^(e - 14), the exponent held to what both powers can express.  The row's largest
+// element then lies in [2^14, 2^15), as high as fp16 lets it: a bf16 element is exact down to 2^-31 of it (its
+// last bit at fp16's last, 2^-24) and off by at most 2^-39 of it below.  (With the largest in [1, 2) elements
+// lost bits from 2^-17 on.)  The raw scores stay below 2^15 * 2688 * 128 < 2^34.
 template <int D>
 __device__ __forceinline__ float kv4_normalise16(const Kv4AttnParams& p, float (&x)[16], int blk, float& norm) {
   if (p.signs) kv4_rotate16<D>(x, p.signs, blk, p.inv_sqrt_d);
@@ -86,9 +89,9 @@ __device__ __forceinline__ float kv4_normalise16(const Kv4AttnParams& p, float (
 #pragma unroll
   for (int o = 1; o < D / kKv4Block; o *= 2) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
   if (am >= 0x7F800000u && blk == 0) atomicOr(p.map.status, DEV_NONFINITE);
-  const int e2 = min(max(int(am >> 23) - 127, -120), 120);
-  norm = __uint_as_float(uint32_t(127 + e2) << 23);
-  return __uint_as_float(uint32_t(127 - e2) << 23);
+  const int e14 = max(int(am >> 23) - 127 - 14, -126);
+  norm = __uint_as_float(uint32_t(127 + e14) << 23);
+  return __uint_as_float(uint32_t(127 - e14) << 23);
 }
 
 // Work is counted in chunks of C tokens of a segment (sequence, KV head, group of R rows),

@@ -196,3 +196,50 @@ def test_binding_refuses_what_32_bits_do_not_hold():
                                ws)
     assert aq.attnq_device_status() == 0
     assert new.item() == -5 and (kept == -5).all() and torch.equal(before, st.cache.pages)
+
+
+@pytest.mark.parametrize("span", [10, 24, 30])
+@pytest.mark.parametrize("T,G,d,out", [(1, 4, 128, BF16), (1, 4, 64, F32), (1, 8, 64, BF16), (9, 2, 128, F32),
+                                       (300, 1, 128, BF16), (300, 1, 64, BF16)])
+def test_bf16_queries_that_span_fp16(T, G, d, out, span):
+    """Unrotated bf16 queries with one element 2^span above the others, in a channel where the keys are 0: the
+    others decide the scores and keep their bits.
+
+    A row enters the products as fp16 with its largest element in [2^14, 2^15), so a bf16 element (8 bits)
+    is exact from 2^-31 of the largest on and off by at most 2^-39 of it below: 2^-39 qmax sum |k| scale of
+    a score, beside d 2^-23 of sum |q k| for the sum's roundings."""
+    aq = _aq()
+    st = Setup([T + 60, T], 2, d, 32, seed=T + span)
+    st.K[..., 7] = 0.0
+    aq.attnq_kv4_append(st.cache, st.seqs, st.K.cuda(), st.V.cuda())
+    gen = torch.Generator().manual_seed(span)
+    Q = torch.randn((2, 2 * G, T, d), generator=gen).to(BF16)
+    Q[..., 7] = 2.0 ** span
+    for weights in (False, True):
+        O = torch.empty(Q.shape, dtype=out, device="cuda")
+        lse = torch.empty(Q.shape[:3], device="cuda") if weights else None
+        acc = torch.zeros((2, 2, st.max_pages * 32), device="cuda") if weights else None
+        ws = torch.empty(aq.attnq_kv4_attn_workspace(st.cache, 2, st.max_pages, 2 * G, T), dtype=torch.uint8,
+                         device="cuda")
+        aq.attnq_kv4_attn(st.cache, aq.AttnqKv4Seqs(st.table, st.lens_t), Q.cuda(), O, True, ws, lse=lse, acc_out=acc)
+        assert aq.attnq_device_status() == 0
+        half, p_err, floor = (2.0 ** -8, 2.0 ** -11, 2.0 ** -32) if out == BF16 else (2.0 ** -24, 2.0 ** -21, 2.0 ** -40)
+        for b, L in enumerate(st.lens):
+            for h in range(2):
+                k, v = st.held(b, h)
+                total, w_tol = torch.zeros(L, dtype=torch.float64), torch.zeros(L, dtype=torch.float64)
+                for hq in range(h * G, (h + 1) * G):
+                    o, l, p, A, bound = ref.attention(Q[b, hq].double(), k, v, d ** -0.5, True)
+                    e_s = bound * (d * 2.0 ** -23 + 2.0 ** -21) + 2.0 ** -21
+                    e_s = e_s + 2.0 ** -39 * 2.0 ** span * k.abs().sum(-1).amax() * d ** -0.5
+                    tol = half * o.abs() + A * (p_err + 2 * e_s + (L + 16) * 2.0 ** -23)[:, None] + floor * v.abs().sum(0)
+                    got = O[b, hq].cpu().double()
+                    assert ((got - o).abs() <= tol).all(), (b, hq, ((got - o).abs() / tol).max())
+                    if weights:
+                        e_l = e_s + (L + 16) * 2.0 ** -23 + 2.0 ** -22 * l.abs()
+                        assert ((lse[b, hq].cpu().double() - l).abs() <= e_l).all()
+                        total += p.sum(0)
+                        w_tol += (p * (2 * e_s + e_l + 2.0 ** -20)[:, None]).sum(0)
+                if weights:
+                    tol = w_tol + total * 2.0 ** -23 * (2 + G * T)
+                    assert ((acc[b, h, :L].cpu().double() - total).abs() <= tol).all()
