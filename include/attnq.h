@@ -458,6 +458,9 @@ attnq_status attnq_kv4_read(const attnq_kv4_cache* cache, const attnq_kv4_seqs* 
  * largest score, or of 2^-31 where O is bf16 and more than 32 rows share a KV head; smaller ones are lost
  * to O, not to lse.  Scores past the fp32 range are unspecified.  A NaN or an
  * infinity in Q is recorded as ATTNQ_ENONFINITE.
+ * Lengths are known on the device only, so the kernels of a call are chosen by what the page table can hold:
+ * a table of at most 4096 places gives small calls (up to 8 rows a KV head) the least latency, and one
+ * whose scores fit the workspace (below) the fastest weights, whatever the lengths are.
  * Two calls on the same inputs give the same bits; in a batch of other lengths the order
  * in which a row's tokens are joined may differ, within these roundings.
  * workspace: DEVICE, 256-byte aligned; needs no initialisation, and calls that overlap need
@@ -487,7 +490,7 @@ attnq_status attnq_kv4_attn(const attnq_kv4_cache* cache, const attnq_kv4_seqs* 
  * [B, Hkv, budget], the ascending old places, -1 behind the last.  acc_out: DEVICE
  * fp32 [B, Hkv, dst_pages * page_tokens] or NULL, the kept tokens' weights (places
  * behind the last are left as they were); not the same array as acc.
- * seqs->new_lens is not looked at.  workspace: DEVICE, 256-byte aligned, at least
+ * seqs->new_lens is not looked at.  Tables of at most 32768 places are thinned fastest.  workspace: DEVICE, 256-byte aligned, at least
  * attnq_kv4_evict_workspace(...) bytes; reserved, nothing is kept in it so far.
  */
 size_t attnq_kv4_evict_workspace(const attnq_kv4_cache* cache, int32_t B, int32_t max_pages, int32_t budget);

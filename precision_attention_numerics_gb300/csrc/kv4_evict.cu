@@ -9,8 +9,9 @@
 // counts of the keys at or above a candidate (about 12 of them): no atomics, and equal weights
 // (a cache has thousands of zeros) cost nothing, where a histogram's atomics
 // on one bin took most of 53 us.  8 x 8 heads of 32768 tokens take 31 us (37 with the threshold
-// built bit by bit and the kept tokens marked one by one), most of it the counts, 2000 clocks each
-// with 1024 threads an SM.  Longer sequences take four histogram passes of 8
+// built bit by bit and the kept tokens marked one by one).  Of a CTA's 47,000 clocks there 11,000 go to loading the
+// weights, 6,000 to their keys, 19,500 to the counts (1,560 each with 1024 threads an SM), 4,000 to marks and
+// prefixes, 1,500 to placing the numbers and 4,000 to the stores.  Longer sequences take four histogram passes of 8
 // bits over memory.  Two block-wide sums then place the kept tokens in order; their
 // numbers go through shared memory, so that the stores are whole lines.
 #include "internal.h"

@@ -27,8 +27,9 @@
 // an SM quadrant, of which the softmax has 1200 and the tiles 700, beside 2048 clocks of MMAs
 // (4 x 128^3 products at 4096 multiply-adds a clock) and 2300 of shared memory (S reads 128 bytes
 // a clock, all there is).  2 x 1024 rows of 32 heads on 16384 tokens (533 GFLOP) take 471 us,
-// 1.13 PFLOP/s, about 3600 clocks a chunk: the chain S, softmax, P V of a row tile and the
-// hand-overs between the roles are what is left.
+// 1.13 PFLOP/s, about 3600 clocks a chunk.  Left are the chain S, softmax, P V of a row tile with the
+// hand-overs between the roles, and what the two roles that give registers away spill (464 to 484 bytes
+// of stores in the compiler's report); how much each costs has not been told apart.
 //
 // Precision: K, V and queries as in kv4_attn.cu, but rotated or fp32 queries are rounded to fp16
 // once, 2^-11, unless lse or weights are asked for (QS: two terms; 2 x 1024 rotated rows as above take 626 us

@@ -243,3 +243,41 @@ def test_bf16_queries_that_span_fp16(T, G, d, out, span):
                 if weights:
                     tol = w_tol + total * 2.0 ** -23 * (2 + G * T)
                     assert ((acc[b, h, :L].cpu().double() - total).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("T,G,out", [(1, 4, BF16), (1, 4, F32), (300, 1, BF16), (300, 1, F32), (150, 4, BF16)])
+def test_weights_near_the_smallest_held(T, G, out):
+    """Most tokens 2^-20 to 2^-36 of a row's largest weight, with values 2^20 times the largest one's.
+
+    P = 2^b p is held in fp16, whose last place is 2^-24: a weight is off by 2^-11 of itself or half of that
+    step, 2^(-25 - b) of the row's largest; b = 15, or 7 in the kernel for many rows with bf16 outputs."""
+    aq = _aq()
+    d, L = 64, 3000
+    st = Setup([L], 1, d, 64, seed=T + G)
+    gen = torch.Generator().manual_seed(T)
+    # constant rows are held as 6 s: one step of s, an eighth of it, is one level of scores
+    level = torch.randint(3, 8, (L,), generator=gen).double()
+    level[17] = 0.0
+    st.K = (12.0 - level[None, None, :, None]).expand(1, 1, L, d).to(BF16).contiguous() * 1.5
+    st.V = torch.randn((1, 1, L, d), generator=gen) * 1024
+    st.V[0, 0, 17] /= 2.0 ** 20
+    st.V = st.V.to(BF16)
+    aq.attnq_kv4_append(st.cache, st.seqs, st.K.cuda(), st.V.cuda())
+    k, v = st.held(0, 0)
+    # one level is 5 to 7 in log2 units: 1.5 d beta scale log2 e
+    beta = (5.0 + 2 * torch.rand((1, G, T, 1), generator=gen)) / (1.5 * d * 0.125 * math.log2(math.e))
+    Q = beta.expand(1, G, T, d).to(BF16)
+    O = torch.empty(Q.shape, dtype=out, device="cuda")
+    ws = torch.empty(aq.attnq_kv4_attn_workspace(st.cache, 1, st.max_pages, G, T), dtype=torch.uint8, device="cuda")
+    aq.attnq_kv4_attn(st.cache, aq.AttnqKv4Seqs(st.table, st.lens_t), Q.cuda(), O, False, ws)
+    assert aq.attnq_device_status() == 0
+    half, p_err, floor = (2.0 ** -8, 2.0 ** -11, 2.0 ** -40) if out == BF16 else (2.0 ** -24, 2.0 ** -21, 2.0 ** -40)
+    if T * G > 32 and out == BF16:
+        floor = 2.0 ** -32
+    for hq in range(G):
+        o, _, p, A, bound = ref.attention(Q[0, hq].double(), k, v, 0.125, False)
+        e_s = bound * (d * 2.0 ** -23 + 2.0 ** -21) + 2.0 ** -21
+        tol = half * o.abs() + A * (p_err + 2 * e_s + (L + 16) * 2.0 ** -23)[:, None]
+        tol = tol + floor * p.amax(-1, keepdim=True) * v.abs().sum(0)
+        assert p.amax() > 0.9 and p.median() < 2.0 ** -20
+        assert ((O[0, hq].cpu().double() - o).abs() <= tol).all(), (hq, ((O[0, hq].cpu().double() - o).abs() / tol).max())
