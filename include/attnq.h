@@ -420,7 +420,8 @@ size_t attnq_kv4_cache_bytes(const attnq_kv4_cache* cache);
  * Quantises the call's rows K, V [B, Hkv, T, d] into their places.  k_mean:
  * DEVICE fp32 [B, Hkv, d], 16-byte aligned, required with ATTNQ_CENTER_K, else NULL.  Other tokens
  * of the pages keep their bits.  A NaN or an infinity is recorded as
- * ATTNQ_ENONFINITE (its block then holds unspecified finite values or NaN).
+ * ATTNQ_ENONFINITE (its block then holds unspecified finite values, or NaN in K; query rows that do
+ * not see the token are not touched by either).
  */
 attnq_status attnq_kv4_append(const attnq_kv4_cache* cache, const attnq_kv4_seqs* seqs, int32_t T,
                               const attnq_rows* K, const attnq_rows* V, const float* k_mean, cudaStream_t stream);

@@ -166,6 +166,9 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv4_append(const AppendParam
     uint32_t s8;
     bool not_finite = false;
     s_code[is_v][r][blk] = quantise16(x, g, s8, not_finite);
+    // a V block with a NaN holds zeros: rows that do not see its token have weight 0 for it, and 0 times a NaN scale
+    // would reach them (their scores against a K block with one are masked)
+    if (is_v && (s8 & 0x7Fu) == 0x7Fu) s8 = 0u;
     s_scale[is_v][r][blk] = uint8_t(s8);
     bad |= not_finite && r >= lo && r < hi;
   }

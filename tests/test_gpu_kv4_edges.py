@@ -281,3 +281,36 @@ def test_weights_near_the_smallest_held(T, G, out):
         tol = tol + floor * p.amax(-1, keepdim=True) * v.abs().sum(0)
         assert p.amax() > 0.9 and p.median() < 2.0 ** -20
         assert ((O[0, hq].cpu().double() - o).abs() <= tol).all(), (hq, ((O[0, hq].cpu().double() - o).abs() / tol).max())
+
+
+@pytest.mark.parametrize("T,G,out", [(4, 1, BF16), (6, 4, F32), (20, 2, BF16), (300, 1, BF16), (300, 1, F32)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_masked_value_that_is_not_finite(T, G, out, bad):
+    """A NaN or an infinity in V or K of the last token is reported when it is written, and rows that do not see
+    that token are as if it were not there (0 times a NaN would be one)."""
+    aq = _aq()
+    st = Setup([T + 70], 2, 64, 16, seed=T)
+    L = T + 70
+    gen = torch.Generator().manual_seed(G)
+    Q = torch.randn((1, 2 * G, T, 64), generator=gen).to(BF16)
+    one = aq.AttnqKv4Seqs(st.table, st.lens_t)
+    for which in "VK":
+        x = {"K": st.K[:, :, -1:].clone(), "V": st.V[:, :, -1:].clone()}
+        x[which][..., 21] = bad
+        aq.attnq_kv4_append(st.cache, one, x["K"].cuda(), x["V"].cuda())
+        assert aq.attnq_device_status() == 4
+        O = torch.empty(Q.shape, dtype=out, device="cuda")
+        lse = torch.empty(Q.shape[:3], device="cuda")
+        ws = torch.empty(aq.attnq_kv4_attn_workspace(st.cache, 1, st.max_pages, 2 * G, T), dtype=torch.uint8, device="cuda")
+        aq.attnq_kv4_attn(st.cache, one, Q.cuda(), O, True, ws, lse=lse)
+        aq.attnq_device_status()
+        half, p_err, floor = (2.0 ** -8, 2.0 ** -11, 2.0 ** -32) if out == BF16 else (2.0 ** -24, 2.0 ** -21, 2.0 ** -40)
+        for hq in range(2 * G):
+            k, v = (t[:L - 1] for t in st.held(0, hq // G))
+            o, l, _, A, bound = ref.attention(Q[0, hq, :T - 1].double(), k, v, 0.125, True)
+            e_s = bound * (64 * 2.0 ** -23 + 2.0 ** -21) + 2.0 ** -21
+            tol = half * o.abs() + A * (p_err + 2 * e_s + (L + 16) * 2.0 ** -23)[:, None] + floor * v.abs().sum(0)
+            assert ((O[0, hq, :T - 1].cpu().double() - o).abs() <= tol).all(), (which, hq)
+            e_l = e_s + (L + 16) * 2.0 ** -23 + 2.0 ** -22 * l.abs()
+            assert ((lse[0, hq, :T - 1].cpu().double() - l).abs() <= e_l).all()
+        aq.attnq_kv4_append(st.cache, one, st.K[:, :, -1:].cuda(), st.V[:, :, -1:].cuda())
