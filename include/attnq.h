@@ -491,8 +491,9 @@ attnq_status attnq_kv4_attn(const attnq_kv4_cache* cache, const attnq_kv4_seqs* 
  * [B, Hkv, budget], the ascending old places, -1 behind the last.  acc_out: DEVICE
  * fp32 [B, Hkv, dst_pages * page_tokens] or NULL, the kept tokens' weights (places
  * behind the last are left as they were); not the same array as acc.
- * seqs->new_lens is not looked at.  Tables of at most 32768 places are thinned fastest.  workspace: DEVICE, 256-byte aligned, at least
- * attnq_kv4_evict_workspace(...) bytes; reserved, nothing is kept in it so far.
+ * seqs->new_lens is not looked at.  Tables of at most 32768 places are thinned fastest.
+ * workspace: DEVICE, 256-byte aligned, at least attnq_kv4_evict_workspace(...) bytes;
+ * reserved, nothing is kept in it so far.
  */
 size_t attnq_kv4_evict_workspace(const attnq_kv4_cache* cache, int32_t B, int32_t max_pages, int32_t budget);
 attnq_status attnq_kv4_evict(const attnq_kv4_cache* cache, const attnq_kv4_seqs* seqs, const float* acc,

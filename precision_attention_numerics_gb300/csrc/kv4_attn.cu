@@ -15,8 +15,9 @@
 //
 // Precision: K and V are exact in fp16, and unrotated bf16 queries down to 2^-31 of their row's largest
 // element (within 2^-39 of it below); rotated or fp32 queries are split into two halves (hi + lo, 22 bits, the
-// same 2^-39 at the least; QS), the second product added in the same accumulators.  P is rounded to fp16 (2^-11 relative, an eighth of
-// the bf16 output's rounding) for bf16 outputs and split in two for fp32 outputs
+// same 2^-39 at the least; QS), the second product added in the same accumulators.
+// P is rounded to fp16 (2^-11 relative, an eighth of the bf16 output's rounding) for
+// bf16 outputs and split in two for fp32 outputs
 // (PS).  Scores, maxima, sums and outputs are fp32.
 #include <cfloat>
 #include <cmath>
